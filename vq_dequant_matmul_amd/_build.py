@@ -11,7 +11,6 @@ import subprocess
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libvqmm.so")
 SOURCES = ["vq_api.cpp", "vq_decode.hip", "vq_decode_d2.hip", "vq_decode_d4.hip",
@@ -28,16 +27,20 @@ COMMON = [
     # keep the compiler from forming packed fp32 instructions
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-function", "-Wno-unknown-pragmas",
-    "-I", os.path.join(ROOT, "include"),
 ]
+
+
+def compile_command(src: str, root: str = ROOT) -> list:
+    """hipcc's command line for one source of the tree at `root`, without what it makes."""
+    package = os.path.basename(HERE)
+    return [HIPCC, "-x", "hip", *COMMON, "-I", os.path.join(root, "include"),
+            os.path.join(root, package, "csrc", src)]
 
 
 def _compile(src: str, extra) -> str:
     obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
-    cmd = [HIPCC, *COMMON, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
-    if src.endswith(".cpp"):
-        cmd[1:1] = ["-x", "hip"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    r = subprocess.run([*compile_command(src), *extra, "-c", "-o", obj], capture_output=True,
+                       text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed for {src}:\n{r.stdout}\n{r.stderr}")
     return obj
@@ -45,6 +48,10 @@ def _compile(src: str, extra) -> str:
 
 def build(extra=(), jobs: int = 8, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
+    # a build that fails leaves no library, and no object that another link could take
+    for old in [LIB] + [os.path.join(BUILD, os.path.splitext(s)[0] + ".o") for s in SOURCES]:
+        if os.path.exists(old):
+            os.remove(old)
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
         objs = list(ex.map(lambda s: _compile(s, list(extra)), SOURCES))
     tmp = LIB + ".tmp"

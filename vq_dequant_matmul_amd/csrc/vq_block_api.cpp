@@ -87,9 +87,9 @@ vq_status check_route(const vq_route_config *c, int32_t n_tokens, vq_dtype logit
         return fail(VQ_ERR_INVALID_ARGUMENT, "cfg is NULL");
     if (c->n_experts < 1)
         return fail(VQ_ERR_INVALID_ARGUMENT, "cfg.n_experts = %d: must be >= 1", c->n_experts);
-    if (c->n_experts > vq::kMaxRouteExperts)
+    if (c->n_experts > vq::kMaxSelectExperts)
         return fail(VQ_ERR_UNSUPPORTED, "cfg.n_experts = %d: at most %d are supported",
-                    c->n_experts, vq::kMaxRouteExperts);
+                    c->n_experts, vq::kMaxSelectExperts);
     if (c->top_k < 1 || c->top_k > c->n_experts)
         return fail(VQ_ERR_INVALID_ARGUMENT, "cfg.top_k = %d: must be in [1, n_experts = %d]",
                     c->top_k, c->n_experts);

@@ -205,7 +205,7 @@ constexpr int kMaxQ4Rows = 1 << 27;    // 256 threads per 16 rows stay under 2^3
 constexpr int kMaxQ4Cols = 1 << 20;    // 32-bit byte offsets inside 16 rows
 constexpr int kMaxRouterRows = 1 << 20; // vq_router_logits: 64 threads per expert
 constexpr int kMaxNormTokens = (1 << 22) - 1;   // 1024 threads per token
-constexpr int kMaxRouteExperts = 1024; // 16 logits a lane
+constexpr int kMaxSelectExperts = 1024; // vq_moe_route: 16 logits a lane
 constexpr int kMaxRouteTopK = 64;      // one slot a lane
 constexpr int kMaxNormHidden = 16384;  // a row in the registers of one workgroup
 

@@ -810,7 +810,7 @@ hipError_t grad_launch(const RouteGradLaunch &L, hipStream_t stream)
 
 size_t route_workspace_bytes(int n_experts, int n_tokens)
 {
-    static_assert(256 + kMaxRouteExperts / kFinishExperts * 16 <= kWsHeader, "header too small");
+    static_assert(256 + kMaxSelectExperts / kFinishExperts * 16 <= kWsHeader, "header too small");
     return kWsHeader + (size_t)route_blocks(n_tokens) * n_experts * 8;
 }
 
