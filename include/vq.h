@@ -406,7 +406,8 @@ typedef struct vq_block_norm_args {
     const void *y;           /* or NULL                                             */
     const void *post_weight; /* [hidden] or NULL                                    */
     const void *pre_weight;  /* [hidden] or NULL for all ones (an offset not added) */
-    const void *gate;        /* [n_tokens] or [hidden], NULL with VQ_GATE_NONE      */
+    const void *gate;        /* [n_tokens] or [hidden], NULL with VQ_GATE_NONE (a gate
+                                per token may be NULL with n_tokens 0)              */
     int32_t gate_kind;       /* VQ_GATE_*                                           */
     float eps;               /* > 0                                                 */
     float weight_offset;     /* 0, or 1 for weights stored as their distance from 1 */

@@ -276,3 +276,25 @@ def test_route_grad_binding_wants_a_matrix_of_ids():
     logits, ids = torch.zeros((2, 8)), torch.zeros(4, dtype=torch.int32)
     with pytest.raises(ValueError, match="topk_ids"):
         vq.vq_moe_route_grad(logits, ids, None)
+
+
+@pytest.mark.parametrize("n", [0, 1, 2])
+def test_norm_channel_gate_is_there_for_any_number_of_tokens(lib, n):
+    """The gradient of the post weight multiplies by the gate, tokens or not."""
+    a = _norm(n_tokens=n, gate_kind=vq.VQ_GATE_CHANNEL, gate=None)
+    for o in ((None, None, FAKE, None, None), (None, None, None, None, FAKE),
+              (None, None, None, FAKE, None)):
+        _refused(lib, lib.vq_block_norm_grad(ctypes.byref(a), FAKE, FAKE, *o, FAKE, 1 << 30, None),
+                 1, "gate")
+    _refused(lib, lib.vq_block_norm(ctypes.byref(a), None), 1, "gate")
+    assert lib.vq_block_norm_grad_workspace_size(ctypes.byref(a)) == 0
+    a.gate_kind, a.gate = vq.VQ_GATE_NONE, FAKE
+    _refused(lib, lib.vq_block_norm(ctypes.byref(a), None), 1, "gate")
+
+
+def test_norm_token_gate_of_no_tokens(lib):
+    """An array with a value per token may be NULL where there are no tokens."""
+    a = _norm(n_tokens=0, gate_kind=vq.VQ_GATE_TOKEN, gate=None)
+    assert lib.vq_block_norm(ctypes.byref(a), None) == 0
+    assert lib.vq_block_norm_grad(ctypes.byref(a), None, None, None, None, None, None, None, None,
+                                  0, None) == 0

@@ -148,7 +148,11 @@ vq_status check_norm(const vq_block_norm_args *a)
         a->gate_kind != VQ_GATE_CHANNEL)
         return fail(VQ_ERR_INVALID_ARGUMENT, "gate_kind = %d: must be one of VQ_GATE_*",
                     a->gate_kind);
-    if ((a->gate_kind != VQ_GATE_NONE) != (a->gate != nullptr) && a->n_tokens > 0)
+    // without tokens the arrays with a row or value per token may be NULL; a gate
+    // per channel may not: its gradient reads it all the same
+    const bool token_gate = a->gate_kind == VQ_GATE_TOKEN;
+    if ((a->gate_kind != VQ_GATE_NONE) != (a->gate != nullptr) &&
+        !(token_gate && a->n_tokens == 0))
         return fail(VQ_ERR_INVALID_ARGUMENT,
                     "gate: must be given with VQ_GATE_TOKEN and VQ_GATE_CHANNEL, and only then");
     if (!a->y && (a->post_weight || a->gate) && a->n_tokens > 0)
