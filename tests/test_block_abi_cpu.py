@@ -298,3 +298,12 @@ def test_norm_token_gate_of_no_tokens(lib):
     assert lib.vq_block_norm(ctypes.byref(a), None) == 0
     assert lib.vq_block_norm_grad(ctypes.byref(a), None, None, None, None, None, None, None, None,
                                   0, None) == 0
+
+
+def test_route_workspace_of_the_largest_batches(lib):
+    """Partial sums are kept for a fixed number of workgroups at most, up to the last int32."""
+    c = ctypes.byref(_route(n_experts=512))
+    most = lib.vq_moe_route_workspace_size(c, 1 << 20)
+    assert most > 512 * 512 * 8
+    for n in (2 ** 31 - 1, 2 ** 31 - 7, 2 ** 31 - 8, 2 ** 31 - 16, 1 << 30):
+        assert lib.vq_moe_route_workspace_size(c, n) == most

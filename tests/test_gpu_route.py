@@ -307,3 +307,20 @@ def test_route_small_scores_in_order(sigmoid, base):
     rows[16:] += step * torch.randint(0, 2, (16, e), generator=g).float() * (rows[16:] < -1)
     ids, _ = vq.vq_moe_route(rows.cuda(), k, score=int(sigmoid), bias=torch.zeros(e).cuda())
     assert torch.equal(ids.cpu().long(), ref.route(rows, k, sigmoid, bias=torch.zeros(e))[0])
+
+
+def test_route_of_the_most_tokens():
+    """2^31 - 1 tokens of one expert: offsets past 32 bits, every element written."""
+    n = 2 ** 31 - 1
+    logits = torch.zeros((n, 1), dtype=torch.bfloat16, device="cuda")
+    ids, w, counts, loss = vq.vq_moe_route(logits, 1, balance=True)
+    # every p is 1: exact in a wave's and a workgroup's sum (below 2^24), then up to
+    # 32 roundings where the workgroups' sums meet
+    assert counts.tolist() == [n] and abs(float(loss) - 1.0) <= 32 * U
+    for out, value in ((ids, 0), (w, 1.0)):
+        assert all((part == value).all() for part in out.split(1 << 28))
+    ids, w = vq.vq_moe_route(logits, 1, score=vq.VQ_SCORE_SIGMOID, renormalize=False)
+    assert all((part == 0).all() for part in ids.split(1 << 28))
+    assert all((part == 0.5).all() for part in w.split(1 << 28))
+    got = vq.vq_moe_route_grad(logits, ids, w, score=vq.VQ_SCORE_SIGMOID, renormalize=False)
+    assert all((part == 0.125).all() for part in got.split(1 << 28))

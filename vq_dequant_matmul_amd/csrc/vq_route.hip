@@ -52,11 +52,14 @@ struct RouteWs {
     int32_t *c;           // [blocks][n_experts]
 };
 
-int route_blocks(int n_tokens)
+// Workgroups of `each` tokens, at most `most`, one at least.
+int blocks_for(int n_tokens, int each, int most)
 {
-    const int b = (n_tokens + kRouteWaves - 1) / kRouteWaves;
-    return b < 1 ? 1 : b > kRouteBlocks ? kRouteBlocks : b;
+    const int64_t b = ((int64_t)n_tokens + each - 1) / each;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(b, most));
 }
+
+int route_blocks(int n_tokens) { return blocks_for(n_tokens, kRouteWaves, kRouteBlocks); }
 
 RouteWs route_ws(void *ws, int n_experts, int blocks)
 {
@@ -798,7 +801,7 @@ hipError_t grad_launch(const RouteGradLaunch &L, hipStream_t stream)
 {
     constexpr int kTokens = kGradWaves * 64 / S;
     // at most eight workgroups per CU (256): each sums the counts first
-    const int blocks = std::min((L.n_tokens + kTokens - 1) / kTokens, 2048);
+    const int blocks = blocks_for(L.n_tokens, kTokens, 2048);
     if (L.logits_bf16)
         k_route_grad<VPL, S, true><<<blocks, 64 * kGradWaves, 0, stream>>>(L);
     else
@@ -817,7 +820,7 @@ size_t route_workspace_bytes(int n_experts, int n_tokens)
 hipError_t launch_route(const RouteLaunch &L, hipStream_t stream)
 {
     const int blocks = L.counts ? route_blocks(L.n_tokens)
-                                : std::min((L.n_tokens + kRouteWaves - 1) / kRouteWaves, 8192);
+                                : blocks_for(L.n_tokens, kRouteWaves, 8192);
     const RouteWs ws = route_ws(L.ws, L.n_experts, blocks);
     hipError_t e = by_width(L.n_experts, L.logits_bf16, [&](auto v, auto bf) {
         k_route<decltype(v)::value, decltype(bf)::value>
