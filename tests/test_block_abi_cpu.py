@@ -307,3 +307,31 @@ def test_route_workspace_of_the_largest_batches(lib):
     assert most > 512 * 512 * 8
     for n in (2 ** 31 - 1, 2 ** 31 - 7, 2 ** 31 - 8, 2 ** 31 - 16, 1 << 30):
         assert lib.vq_moe_route_workspace_size(c, n) == most
+
+
+def _wide_block(hidden, inter, d=4, bits=9):
+    K = 1 << bits
+    t = [vq._CTensor(r, c, d, bits, K, 4, 4 * r, FAKE, FAKE, FAKE, None)
+         for r, c in ((inter, hidden), (inter, hidden), (hidden, inter))]
+    none = ctypes.POINTER(vq._CQ4)()
+    return vq._CBlock(*(ctypes.pointer(x) for x in t), none, none, none, FAKE, None,
+                      _route(n_experts=4, top_k=2), 1, 0, FAKE, None, None, 1e-6, 0.0, 1.0, 1.0)
+
+
+@pytest.mark.parametrize("hidden,inter,n,needle", [
+    (8256, 64, 1, "columns"), (64, 8256, 1, "columns"), (8256, 64, 16, "columns"),
+    (16448, 64, 17, "norms"), (16448, 64, 1, "columns"),
+])
+def test_block_refuses_sizes_of_a_later_step_before_any(lib, hidden, inter, n, needle):
+    """The routed FFN's limits and the norms' are checked ahead of the first
+    step, which updates h: no launch is tried (without a GPU that would be
+    VQ_ERR_HIP), and there is no workspace for such a call."""
+    b = ctypes.byref(_wide_block(hidden, inter))
+    assert lib.vq_moe_block_workspace_size(b, n) == 0
+    _refused(lib, lib.vq_moe_block(b, n, FAKE, FAKE, None, None, None, FAKE, 1 << 34, None), 2,
+             needle)
+
+
+def test_block_sizes_at_the_limits(lib):
+    for hidden, inter, n in ((8192, 8192, 1), (8256, 64, 17), (64, 8256, 64)):
+        assert lib.vq_moe_block_workspace_size(ctypes.byref(_wide_block(hidden, inter)), n) > 0

@@ -608,6 +608,31 @@ static vq_status run_decode_ffn(const vq::TensorDev &g, const vq::TensorDev &u,
     return e == hipSuccess ? ok() : hip_fail(e, what);
 }
 
+// Limits of the engine that runs the call.
+static vq_status check_ffn_sizes(const vq_tensor &gate, const vq_tensor &down, int32_t n_tokens,
+                                 int32_t top_k)
+{
+    if (ffn_uses_decode(gate, down, n_tokens, top_k))
+        return check_decode_sizes(gate, down, n_tokens, top_k);
+    const vq_status st = check_prefill_sizes(gate, n_tokens, top_k);
+    if (st != VQ_OK)
+        return st;
+    if (!vq::moe_prefill_fits(vq::to_dev(gate), vq::to_dev(down), n_tokens, top_k))
+        return fail(VQ_ERR_UNSUPPORTED, "vq_moe_ffn: geometry not supported by the MFMA path");
+    return VQ_OK;
+}
+
+namespace vq {
+
+vq_status check_moe_ffn(const vq_tensor *gate, const vq_tensor *up, const vq_tensor *down,
+                        int32_t n_tokens, int32_t top_k)
+{
+    const vq_status st = check_ffn(gate, up, down, n_tokens, top_k);
+    return st != VQ_OK || n_tokens == 0 ? st : check_ffn_sizes(*gate, *down, n_tokens, top_k);
+}
+
+}  // namespace vq
+
 VQ_EXPORT size_t vq_moe_ffn_workspace_size(const vq_tensor *gate, const vq_tensor *up,
                                            const vq_tensor *down, int32_t n_tokens, int32_t top_k)
 {
@@ -655,9 +680,9 @@ VQ_EXPORT vq_status vq_moe_ffn(const vq_tensor *gate, const vq_tensor *up, const
     hipStream_t s = static_cast<hipStream_t>(stream);
     const vq::TensorDev g = vq::to_dev(*gate), u = vq::to_dev(*up), dn = vq::to_dev(*down);
 
+    if ((st = check_ffn_sizes(*gate, *down, n_tokens, top_k)) != VQ_OK)
+        return st;
     if (!ffn_uses_decode(*gate, *down, n_tokens, top_k)) {
-        if ((st = check_prefill_sizes(*gate, n_tokens, top_k)) != VQ_OK)
-            return st;
         const size_t need = vq::moe_prefill_workspace_bytes(g, u, dn, n_tokens, top_k);
         if (!workspace || workspace_bytes < need || !aligned(workspace, 256))
             return fail(VQ_ERR_WORKSPACE,
@@ -665,14 +690,10 @@ VQ_EXPORT vq_status vq_moe_ffn(const vq_tensor *gate, const vq_tensor *up, const
                         workspace_bytes, workspace);
         hipError_t e = vq::launch_moe_prefill(g, u, dn, n_tokens, top_k, x, x_dtype == VQ_F32,
                                               topk_ids, topk_weights, y, workspace, s);
-        if (e == hipErrorNotSupported)
-            return fail(VQ_ERR_UNSUPPORTED, "vq_moe_ffn: geometry not supported by the MFMA path");
         return e == hipSuccess ? ok() : hip_fail(e, "vq_moe_ffn (prefill)");
     }
 
     // ---- decode: gate+up+SwiGLU -> down -> slot-ordered combine ------------------
-    if ((st = check_decode_sizes(*gate, *down, n_tokens, top_k)) != VQ_OK)
-        return st;
     const DecodeWs ws = decode_ws(*gate, *down, n_tokens, top_k);
     if (!workspace || workspace_bytes < ws.total || !aligned(workspace, 256))
         return fail(VQ_ERR_WORKSPACE,

@@ -411,13 +411,16 @@ vq_status check_block(const vq_moe_block_args *B, int32_t n_tokens, BlockWs *ws)
     if (n_tokens < 0 || n_tokens > vq::kDenseMaxTokens)
         return fail(VQ_ERR_INVALID_ARGUMENT, "n_tokens = %d: must be in [0, %d]", n_tokens,
                     vq::kDenseMaxTokens);
-    // (the FFN's own checks, on every tensor of it)
-    int32_t engine;
-    vq_status st = vq_moe_ffn_engine(B->gate, B->up, B->down, n_tokens, B->route.top_k, &engine);
+    // (the FFN's own checks, all of them: nothing runs, and h stays as it is,
+    // where a later step would refuse the sizes)
+    vq_status st = vq::check_moe_ffn(B->gate, B->up, B->down, n_tokens, B->route.top_k);
     if (st != VQ_OK || (st = check_route(&B->route, n_tokens, VQ_F32)) != VQ_OK ||
         (st = check_float_dtype(B->x_dtype, "x_dtype")) != VQ_OK)
         return st;
     const int hidden = B->gate->cols;
+    if (hidden > vq::kMaxNormHidden)
+        return fail(VQ_ERR_UNSUPPORTED, "gate.cols = %d: the norms take at most %d", hidden,
+                    vq::kMaxNormHidden);
     if (B->route.n_experts != B->gate->n_experts)
         return fail(VQ_ERR_INVALID_ARGUMENT, "route.n_experts = %d but gate has %d experts",
                     B->route.n_experts, B->gate->n_experts);
@@ -449,12 +452,9 @@ vq_status check_block(const vq_moe_block_args *B, int32_t n_tokens, BlockWs *ws)
     ws->y = ws->weights + round_up(n * k * 4);
     ws->shared = ws->y + round_up(n * hidden * 4);
     ws->ffn = ws->shared + (shared ? round_up(n * B->shared_gate->rows * 4) : 0);
-    size_t ffn = 0;
-    if (n_tokens > 0) {
-        ffn = vq_moe_ffn_workspace_size(B->gate, B->up, B->down, n_tokens, B->route.top_k);
-        if (ffn == 0)
-            return fail(VQ_ERR_UNSUPPORTED, "%d tokens: not supported by the routed FFN", n_tokens);
-    }
+    const size_t ffn =
+        n_tokens == 0 ? 0
+                      : vq_moe_ffn_workspace_size(B->gate, B->up, B->down, n_tokens, B->route.top_k);
     ws->total = ws->ffn + round_up(ffn);
     return VQ_OK;
 }

@@ -102,6 +102,8 @@ hipError_t launch_expert_gemm(const TensorDev &t, int n_x_rows, const void *x, i
                               hipStream_t stream);
 size_t moe_prefill_workspace_bytes(const TensorDev &g, const TensorDev &u, const TensorDev &dn,
                                    int n_tok, int top_k);
+// (whether the grouped GEMM holds the experts' geometry)
+bool moe_prefill_fits(const TensorDev &g, const TensorDev &dn, int n_tok, int top_k);
 hipError_t launch_moe_prefill(const TensorDev &g, const TensorDev &u, const TensorDev &dn,
                               int n_tok, int top_k, const void *x, int x_f32,
                               const int32_t *ids, const float *w, float *y, void *ws,

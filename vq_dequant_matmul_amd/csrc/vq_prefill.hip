@@ -565,16 +565,20 @@ size_t moe_prefill_workspace_bytes(const TensorDev &g, const TensorDev &, const 
     return ffn_ws(g, dn, n_tok, top_k).total;
 }
 
+bool moe_prefill_fits(const TensorDev &g, const TensorDev &dn, int n_tok, int top_k)
+{
+    if (g.n_experts > kMaxRouteExperts)
+        return false;
+    const int mb = ffn_ws(g, dn, n_tok, top_k).mb;
+    return gemm_fits(g.d, g.bits, 1, mb, g.rows, g.groups) &&
+           gemm_fits(dn.d, dn.bits, 1, mb, dn.rows, dn.groups);
+}
+
 hipError_t launch_moe_prefill(const TensorDev &g, const TensorDev &u, const TensorDev &dn,
                               int n_tok, int top_k, const void *x, int x_f32, const int32_t *ids,
                               const float *wts, float *y, void *ws, hipStream_t stream)
 {
-    if (g.n_experts > kMaxRouteExperts)
-        return hipErrorNotSupported;
     const FfnWs w = ffn_ws(g, dn, n_tok, top_k);
-    if (!gemm_fits(g.d, g.bits, 1, w.mb, g.rows, g.groups) ||
-        !gemm_fits(dn.d, dn.bits, 1, w.mb, dn.rows, dn.groups))
-        return hipErrorNotSupported;
     char *base = static_cast<char *>(ws);
     int32_t *offs = reinterpret_cast<int32_t *>(base + w.offs);
     int32_t *perm = reinterpret_cast<int32_t *>(base + w.perm);
