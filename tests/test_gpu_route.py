@@ -324,3 +324,41 @@ def test_route_of_the_most_tokens():
     assert all((part == 0.5).all() for part in w.split(1 << 28))
     got = vq.vq_moe_route_grad(logits, ids, w, score=vq.VQ_SCORE_SIGMOID, renormalize=False)
     assert all((part == 0.125).all() for part in got.split(1 << 28))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("parts", ["weights", "loss"])
+def test_sigmoid_gradient_of_large_logits(dtype, renorm, parts):
+    """Scores next to 1: the gradient's factor 1 - s is as exact as the rest, so
+    the bound scales with it."""
+    t, e, k, dl = 50, 72, 6, 40.0
+    g = torch.Generator().manual_seed(12)
+    logits = (10 + 20 * torch.rand((t, e), generator=g)).to(dtype)
+    logits[::3, 1::2] *= -1
+    ids, _, counts, _ = ref.route(logits, k, True, renorm)
+    dw = torch.randn((t, k), generator=g) if parts == "weights" else None
+    counts = counts if parts == "loss" else None
+    got = vq.vq_moe_route_grad(
+        logits.cuda(), ids.int().cuda(), _c(dw), score=vq.VQ_SCORE_SIGMOID, renormalize=renorm,
+        counts=None if counts is None else counts.int().cuda(),
+        d_loss=None if counts is None else torch.tensor([dl]).cuda())
+    l = d(logits)
+    s, rest = torch.sigmoid(l), torch.sigmoid(-l)     # rest = 1 - s
+    if parts == "weights":
+        w = ref.weights(l, ids, True, renorm, 1.0)
+        a = d(dw) * w
+        sub = w * a.sum(1, keepdim=True) if renorm else 0.0 * a
+        want = torch.zeros_like(l).scatter_add(1, ids, a - sub) * rest
+        mag = torch.zeros_like(l).scatter_add(1, ids, a.abs() + (
+            w * a.abs().sum(1, keepdim=True) if renorm else 0.0)) * rest
+    else:
+        p = s / s.sum(1, keepdim=True)
+        f = dl * e * counts.double() / counts.sum() / t
+        want = p * (f - (p * f).sum(1, keepdim=True)) * rest
+        mag = p * (f + (p * f).sum(1, keepdim=True)) * rest
+    # two exponentials, each off by its argument's half step (|logit| <= 30) and
+    # its own, twice as much for the fast ones; sums of e terms in lanes, products
+    bound = (4 * (30 + 4) + e / 16 + 6 + 20) * U * mag + HALF_STEP[dtype] * want.abs() + 1e-37
+    err = (d(got) - want).abs()
+    assert (err <= bound).all(), (err / bound).max()

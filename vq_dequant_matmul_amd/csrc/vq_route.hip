@@ -198,7 +198,15 @@ __device__ __forceinline__ void store_logits(void *p, int64_t row, int E, int e0
     }
 }
 
-__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
+// FAST: the hardware's exp2 and reciprocal.
+template <bool FAST = false>
+__device__ __forceinline__ float sigmoid(float v)
+{
+    if constexpr (FAST)
+        return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * v));
+    else
+        return 1.0f / (1.0f + expf(-v));
+}
 
 // The lane's scores, p = score * inv (0 where no score is above 0), and the
 // row's largest logit and sum of exponentials for the softmax.  FAST: the
@@ -221,8 +229,7 @@ __device__ __forceinline__ void scores(bool sig, const float (&l)[VPL], float (&
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
         if constexpr (FAST)
-            s[j] = sig ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * l[j]))
-                       : __builtin_amdgcn_exp2f(kLog2e * (l[j] - top));
+            s[j] = sig ? sigmoid<true>(l[j]) : __builtin_amdgcn_exp2f(kLog2e * (l[j] - top));
         else
             s[j] = sig ? sigmoid(l[j]) : expf(l[j] - top);
         total += s[j];
@@ -771,7 +778,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_route_grad(RouteGradLaunch 
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
             if (sig)
-                d[j] *= 1.0f - s[j];
+                d[j] *= sigmoid<BF16>(-l[j]);   // 1 - s, without its cancellation near s = 1
             if (l[j] == kNegInf || !live)
                 d[j] = 0.0f;
         }
