@@ -362,3 +362,20 @@ def test_sigmoid_gradient_of_large_logits(dtype, renorm, parts):
     bound = (4 * (30 + 4) + e / 16 + 6 + 20) * U * mag + HALF_STEP[dtype] * want.abs() + 1e-37
     err = (d(got) - want).abs()
     assert (err <= bound).all(), (err / bound).max()
+
+
+@pytest.mark.parametrize("base", [-80.0, -40.0, 30.0])
+def test_loss_of_sigmoid_scores_far_from_0(base):
+    """One token, whose choice the bias makes: the loss is n_experts * p of that
+    expert, and p is as exact far from a logit of 0 as near it."""
+    e = 8
+    bias = torch.zeros(e)
+    bias[3] = 10.0
+    for seed in range(48):
+        logits = base + torch.randn((1, e), generator=torch.Generator().manual_seed(seed))
+        loss = vq.vq_moe_route(logits.cuda(), 1, score=vq.VQ_SCORE_SIGMOID, bias=bias.cuda(),
+                               balance=True)[3]
+        want = float(ref.route(logits, 1, True, bias=bias)[3])
+        # a score: exp 4, its sum with 1 and the reciprocal 3, own and in the sum; the
+        # sum over 8 experts, its reciprocal, the product and the result, in half steps
+        assert abs(float(loss) - want) <= (7 + 7 + 7 + 4) * U * want, seed

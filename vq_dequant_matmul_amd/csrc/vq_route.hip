@@ -198,26 +198,37 @@ __device__ __forceinline__ void store_logits(void *p, int64_t row, int E, int e0
     }
 }
 
-// FAST: the hardware's exp2 and reciprocal.
+// exp(x) by the hardware's exp2 at x log2(e), with what the product's rounding and
+// the constant's leave out, d: 2^hi (1 + d ln 2), 2^-22 relative.  (Without that
+// term the error grows with |x|, to 5e-6 at 80.)  Infinities of x make d NaN,
+// which the median turns into a bound that changes no 0 and no infinity.
+__device__ __forceinline__ float exp_fast(float x)
+{
+    constexpr float kLog2e = 0x1.715476p+0f, kLog2eLow = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
+    const float hi = kLog2e * x;
+    const float d = fmaf(kLog2eLow, x, fmaf(kLog2e, x, -hi));
+    return __builtin_amdgcn_exp2f(hi) *
+           fmaf(kLn2, __builtin_amdgcn_fmed3f(d, -0x1p-10f, 0x1p-10f), 1.0f);
+}
+
+// FAST: exp_fast and the hardware's reciprocal.
 template <bool FAST = false>
 __device__ __forceinline__ float sigmoid(float v)
 {
     if constexpr (FAST)
-        return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * v));
+        return __builtin_amdgcn_rcpf(1.0f + exp_fast(-v));
     else
         return 1.0f / (1.0f + expf(-v));
 }
 
 // The lane's scores, p = score * inv (0 where no score is above 0), and the
-// row's largest logit and sum of exponentials for the softmax.  FAST: the
-// hardware's exp2 and reciprocal, relative error (|logit| + 4) 2^-23 (for the
-// order, which near ties decide in 64 bits, for the loss, and for gradients
-// that are rounded to bf16); else a few 2^-24.
+// row's largest logit and sum of exponentials for the softmax.  Relative error
+// a few 2^-24, with FAST (the order, which near ties decide in 64 bits, the loss
+// and gradients that are rounded to bf16) a few 2^-23.
 template <int VPL, int S, bool FAST>
 __device__ __forceinline__ void scores(bool sig, const float (&l)[VPL], float (&s)[VPL],
                                        float &inv, float &top, float &total)
 {
-    constexpr float kLog2e = 1.44269504f;
     top = kNegInf;
     total = 0.0f;
     if (!sig) {
@@ -228,10 +239,7 @@ __device__ __forceinline__ void scores(bool sig, const float (&l)[VPL], float (&
     }
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
-        if constexpr (FAST)
-            s[j] = sig ? sigmoid<true>(l[j]) : __builtin_amdgcn_exp2f(kLog2e * (l[j] - top));
-        else
-            s[j] = sig ? sigmoid(l[j]) : expf(l[j] - top);
+        s[j] = sig ? sigmoid<FAST>(l[j]) : FAST ? exp_fast(l[j] - top) : expf(l[j] - top);
         total += s[j];
     }
     total = segment_sum<S>(total);
@@ -390,10 +398,8 @@ __device__ __noinline__ int select_all(const float *logit, const float *bias, bo
 // before them.  (One maximum of the wave per slot instead took two and a half
 // times the instructions, most of them on the one scalar unit of a CU.)
 //
-// With a bias a key is off by up to kNear * (|key| + bias_max) / 2 (the scores
-// by up to 2^-16 of them: logits, or their distance from the largest, of up to
-// 87, past which an fp32 score is 0, plus 4, times 2^-23; and the rounding of
-// the sum): what is within kNear of the bound is a candidate too, and if two
+// With a bias a key is off by less than kNear * (|key| + bias_max) / 2 (the
+// scores by a few 2^-23 of them, and the rounding of the sum): what is within kNear of the bound is a candidate too, and if two
 // neighbours among the first k + 1 are, the candidates are ordered by 64-bit
 // keys.
 template <int VPL>
