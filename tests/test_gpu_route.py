@@ -379,3 +379,30 @@ def test_loss_of_sigmoid_scores_far_from_0(base):
         # a score: exp 4, its sum with 1 and the reciprocal 3, own and in the sum; the
         # sum over 8 experts, its reciprocal, the product and the result, in half steps
         assert abs(float(loss) - want) <= (7 + 7 + 7 + 4) * U * want, seed
+
+
+@pytest.mark.parametrize("t", [1 << 16, (1 << 24) + 5])
+def test_loss_of_equal_tokens(t):
+    """The same p of every token: a rounding of one addition repeats in all."""
+    e, k = 3, 1
+    logits = torch.zeros((t, e), device="cuda")
+    ids, _, counts, loss = vq.vq_moe_route(logits, k, balance=True)
+    assert counts.tolist() == [t, 0, 0]
+    # loss = 3 * p[0]: p has 3 roundings, 16 tokens are added in fp32, a workgroup's
+    # sum and the result are rounded once
+    assert abs(float(loss) - 1.0) <= (3 + 16 + 2) * U
+
+
+def test_loss_shows_a_nan():
+    """A NaN logit of one token that counts, wherever it is, and of one that does not."""
+    t, e = 5000, 130
+    logits = _logits(t, e, torch.float32, 3)
+    for sigmoid in (0, 1):
+        for row in (0, 17, 4999):
+            bad = logits.clone()
+            bad[row, 77] = NAN
+            mask = torch.ones(t, dtype=torch.bool)
+            assert vq.vq_moe_route(bad.cuda(), 4, score=sigmoid, balance=True)[3].isnan().all()
+            mask[row] = False
+            loss = vq.vq_moe_route(bad.cuda(), 4, score=sigmoid, mask=mask.cuda(), balance=True)[3]
+            assert torch.isfinite(loss).all()

@@ -474,11 +474,38 @@ __device__ __forceinline__ int select(const uint32_t (&key)[VPL], RouteRow<VPL> 
     return out;
 }
 
+// The sums of p over tokens: fp32 over kHeld tokens of a wave; where a wave has
+// more, whole numbers of 2^-40 in LDS for the workgroup (whose order does not
+// matter; at most 2^22 tokens, 2^62); 64 bits over the waves' last ones and the
+// workgroups, with one rounding to fp32 between.  (Whole numbers for the last
+// ones too: 4096x512 19.8 us, else 19.3.)
+constexpr int kHeld = 16;
+
+template <int VPL>
+__device__ __forceinline__ void flush_sums(float (&psum)[VPL], unsigned long long *sums, bool *bad)
+{
+    const int lane = threadIdx.x & 63;
+    bool nan = false;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+        nan |= psum[j] != psum[j];
+        // below 2^52: the number is in the mantissa
+        const double v = fma((double)psum[j], 0x1p40, 0x1p52);
+        atomicAdd(&sums[j * 64 + lane],
+                  (unsigned long long)__double_as_longlong(v) & 0xfffffffffffffull);
+        psum[j] = 0.0f;
+    }
+    if (nan)
+        *bad = true;
+}
+
 template <int VPL, bool BF16>
 __global__ __launch_bounds__(64 * kRouteWaves, VPL <= 8 ? 4 : 2) void k_route(RouteLaunch L, RouteWs ws)
 {
     __shared__ RouteRow<VPL> rows[kRouteWaves];   // at last, the sums of p in place of logits
+    __shared__ unsigned long long lp[64 * VPL];   // [VPL][64]: a lane's experts apart
     __shared__ int lc[64 * VPL];
+    __shared__ bool bad;                          // a NaN among the p
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, E = L.n_experts, k = L.top_k;
     const int e0 = lane * VPL;
     const bool stats = L.counts != nullptr, sig = L.sigmoid;
@@ -487,8 +514,12 @@ __global__ __launch_bounds__(64 * kRouteWaves, VPL <= 8 ? 4 : 2) void k_route(Ro
     if (stats) {
         if (blockIdx.x == 0 && threadIdx.x == 0)
             *ws.ticket = 0;
-        for (int i = threadIdx.x; i < 64 * VPL; i += 64 * kRouteWaves)
+        if (threadIdx.x == 0)
+            bad = false;
+        for (int i = threadIdx.x; i < 64 * VPL; i += 64 * kRouteWaves) {
             lc[i] = 0;
+            lp[i] = 0;
+        }
         __syncthreads();
     }
     float bias[VPL], bias_max = 0.0f;
@@ -501,8 +532,14 @@ __global__ __launch_bounds__(64 * kRouteWaves, VPL <= 8 ? 4 : 2) void k_route(Ro
         bias_max = segment_max<64>(bias_max);
     }
     float psum[VPL] = {};
-    for (int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave; t < L.n_tokens;
-         t += (int64_t)gridDim.x * kRouteWaves) {
+    const int64_t first = (int64_t)blockIdx.x * kRouteWaves + wave;
+    const int64_t step = (int64_t)gridDim.x * kRouteWaves;
+    int64_t flush_at = first + kHeld * step;
+    for (int64_t t = first; t < L.n_tokens; t += step) {
+        if (stats && t == flush_at) {
+            flush_sums(psum, lp, &bad);
+            flush_at += kHeld * step;
+        }
         float l[VPL];
         load_logits<VPL, BF16>(L.logits, t, E, e0, by_four, l);
         bool some = false;
@@ -563,10 +600,10 @@ __global__ __launch_bounds__(64 * kRouteWaves, VPL <= 8 ? 4 : 2) void k_route(Ro
         rows[wave].logit[e0 + j] = psum[j];
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += 64 * kRouteWaves) {
-        float v = 0.0f;
+        double v = (double)lp[e % VPL * 64 + e / VPL] * 0x1p-40;
         for (int w = 0; w < kRouteWaves; ++w)
             v += rows[w].logit[e];
-        ws.p[(size_t)blockIdx.x * E + e] = v;
+        ws.p[(size_t)blockIdx.x * E + e] = bad ? __builtin_nanf("") : (float)v;
         ws.c[(size_t)blockIdx.x * E + e] = lc[e];
     }
 }
@@ -578,12 +615,12 @@ __global__ __launch_bounds__(1024) void k_route_finish(RouteWs ws, int blocks, i
                                                        int32_t *counts, float *loss)
 {
     constexpr int kRows = 1024 / kFinishExperts, kAtOnce = 8;
-    __shared__ float lp[kRows][kFinishExperts];
+    __shared__ double lp[kRows][kFinishExperts];
     __shared__ int lc[kRows][kFinishExperts];
     __shared__ bool last;
     const int col = threadIdx.x % kFinishExperts, row = threadIdx.x / kFinishExperts;
     const int e = blockIdx.x * kFinishExperts + col;
-    float p = 0.0f;
+    double p = 0.0;
     int c = 0;
     if (e < E)
         for (int b0 = row; b0 < blocks; b0 += kRows * kAtOnce) {
@@ -614,7 +651,7 @@ __global__ __launch_bounds__(1024) void k_route_finish(RouteWs ws, int blocks, i
     __syncthreads();
     if (threadIdx.x < 64) {
         const bool mine = threadIdx.x < kFinishExperts && e < E;
-        p = mine ? lp[0][col] : 0.0f;
+        p = mine ? lp[0][col] : 0.0;
         c = mine ? lc[0][col] : 0;
         if (mine)
             counts[e] = c;
