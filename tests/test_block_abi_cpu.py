@@ -335,3 +335,35 @@ def test_block_refuses_sizes_of_a_later_step_before_any(lib, hidden, inter, n, n
 def test_block_sizes_at_the_limits(lib):
     for hidden, inter, n in ((8192, 8192, 1), (8256, 64, 17), (64, 8256, 64)):
         assert lib.vq_moe_block_workspace_size(ctypes.byref(_wide_block(hidden, inter)), n) > 0
+
+
+def test_binding_refuses_tensors_that_need_a_history():
+    """The results have no history: with grad enabled a backward pass would leave
+    these inputs out without a word."""
+    p = torch.nn.Parameter
+    h, w, l = torch.zeros((2, 64)), torch.ones(64), torch.zeros((2, 8))
+    with pytest.raises(ValueError, match="vq_moe_route_grad"):
+        vq.vq_moe_route(p(l), 2)
+    for kw in (dict(h=p(h)), dict(h=h, y=p(h)), dict(h=h, y=h, post_weight=p(w)),
+               dict(h=h, pre_weight=p(w)), dict(h=h, y=h, gate=p(w))):
+        with pytest.raises(ValueError, match="vq_block_norm_grad"):
+            vq.vq_block_norm(**kw)
+    r = torch.zeros((8, 64), dtype=torch.bfloat16)
+    for a in ((p(r), h), (r, p(h))):
+        with pytest.raises(ValueError, match="history"):
+            vq.vq_router_logits(*a)
+    q = vq.VQQ4Tensor(4, 64, 64, torch.zeros((4, 8), dtype=torch.int32),
+                      torch.zeros((4, 1), dtype=torch.float16))
+    with pytest.raises(ValueError, match="history"):
+        vq.vq_q4_gemv(q, p(h))
+    with pytest.raises(ValueError, match="history"):
+        vq.vq_q4_gate_up(q, q, p(h))
+
+
+def test_binding_without_grad_takes_parameters():
+    """Under no_grad the same tensors go on to the checks behind (here: no GPU)."""
+    h = torch.nn.Parameter(torch.zeros((2, 64)))
+    with torch.no_grad():
+        for call in (lambda: vq.vq_block_norm(h), lambda: vq.vq_moe_route(h, 2)):
+            with pytest.raises((TypeError, RuntimeError)):
+                call()

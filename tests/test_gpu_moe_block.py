@@ -160,3 +160,19 @@ def test_router_training_step():
         # fp32 products of up to 256 terms in a chain: 256 half steps of the
         # largest sums, with room for the two products in a row
         assert (d(got) - want).norm() <= 2 * 256 * ref.U * want.norm() + 1e-12
+
+
+def test_block_refuses_tensors_that_need_a_history():
+    hidden, n = 256, 2
+    b, _, _ = _block(17, 8, 2, hidden, 64)
+    h, nw = _r((n, hidden), F, 1).cuda(), torch.ones(hidden, device="cuda")
+    keep = h.clone()
+    for kw in (dict(h=torch.nn.Parameter(h)), dict(h=h, attn=torch.nn.Parameter(h)),
+               dict(h=h, next_weight=torch.nn.Parameter(nw))):
+        with pytest.raises(ValueError, match="history"):
+            vq.vq_moe_block(b, **kw)
+    assert torch.equal(h, keep)
+    want = vq.vq_moe_block(b, h.clone(), next_weight=nw)
+    with torch.no_grad():
+        got = vq.vq_moe_block(b, h, next_weight=torch.nn.Parameter(nw))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -520,7 +520,8 @@ def vq_moe_combine(z: torch.Tensor, topk_weights: torch.Tensor,
 #
 # One token's call runs a few microseconds on the GPU, so these bindings keep
 # the host's part short: descriptors are built once, pointers go to ctypes as
-# plain integers.
+# plain integers.  They record no autograd history and refuse tensors that would
+# need one (the gradients that there are have calls of their own).
 
 _DTYPE = {torch.float32: VQ_F32, torch.bfloat16: VQ_BF16}
 _F32 = torch.float32
@@ -552,6 +553,14 @@ def _same_device(device, **tensors):
     for name, t in tensors.items():
         if t is not None and t.device != device:
             raise ValueError(f"{name} is on {t.device}, the other arguments on {device}")
+
+
+def _refuse_history(name, gradient=None):
+    """For tensors that require grad: what these calls return has no history, and
+    a backward pass would leave them out without a word."""
+    if torch.is_grad_enabled():
+        raise ValueError(f"{name} records no autograd history: call it under torch.no_grad()" +
+                         (f" and take the gradient from {gradient}" if gradient else ""))
 
 
 def _addr(t: Optional[torch.Tensor]):
@@ -631,7 +640,9 @@ class VQQ4Tensor:
         return self.codes.numel() * 4 + self.scales.numel() * (2 if self.biases is None else 4)
 
 
-def _dense_x(x, cols, device):
+def _dense_x(name, x, cols, device):
+    if x.requires_grad:
+        _refuse_history(name)
     if x.dim() != 2 or x.shape[1] != cols:
         raise ValueError(f"x must be [n_tokens, {cols}], got {tuple(x.shape)}")
     if x.device != device:
@@ -643,7 +654,7 @@ def vq_q4_gemv(W: VQQ4Tensor, x: torch.Tensor, out: Optional[torch.Tensor] = Non
                accumulate: bool = False) -> torch.Tensor:
     """y[n] = W x[n] for up to 64 tokens, fp32 [n_tokens, rows]; with
     accumulate the product is added to what `out` holds."""
-    x = _dense_x(x, W.cols, W.device)
+    x = _dense_x("vq_q4_gemv", x, W.cols, W.device)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     n = x.shape[0]
@@ -656,7 +667,7 @@ def vq_q4_gemv(W: VQQ4Tensor, x: torch.Tensor, out: Optional[torch.Tensor] = Non
 def vq_q4_gate_up(gate: VQQ4Tensor, up: VQQ4Tensor, x: torch.Tensor,
                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """h[n] = silu(W_gate x[n]) * (W_up x[n]) for up to 64 tokens, fp32."""
-    x = _dense_x(x, gate.cols, gate.device)
+    x = _dense_x("vq_q4_gate_up", x, gate.cols, gate.device)
     if up.device != gate.device:
         raise ValueError(f"up is on {up.device}, gate on {gate.device}")
     n = x.shape[0]
@@ -672,8 +683,10 @@ def vq_router_logits(w: torch.Tensor, x: torch.Tensor,
     up to 64 tokens, fp32."""
     if w.dtype != torch.bfloat16 or w.dim() != 2 or not w.is_contiguous():
         raise TypeError("w must be a contiguous bfloat16 tensor [n_experts, hidden]")
+    if w.requires_grad:
+        _refuse_history("vq_router_logits")
     e, hidden = w.shape
-    x = _dense_x(x, hidden, w.device)
+    x = _dense_x("vq_router_logits", x, hidden, w.device)
     n = x.shape[0]
     out = _out(out, (n, e), _F32, w.device)
     _on_device(x, load_library().vq_router_logits, e, hidden, w.data_ptr(), n, x.data_ptr(),
@@ -710,6 +723,8 @@ def vq_moe_route(logits: torch.Tensor, top_k: int, *, score: int = VQ_SCORE_SOFT
     """Each token's top_k experts and their weights (see vq.h, vq_moe_route):
     (ids int32, weights fp32), both [n_tokens, top_k]; with balance also
     (counts int32 [n_experts], loss fp32 [1])."""
+    if logits.requires_grad:
+        _refuse_history("vq_moe_route", "vq_moe_route_grad")
     _check_logits(logits, mask)
     n, e = logits.shape
     dev = logits.device
@@ -807,6 +822,11 @@ def vq_block_norm(h: torch.Tensor, y: Optional[torch.Tensor] = None, *,
     h, y: [n_tokens, hidden] fp32 or bf16, rows may be strided; post_weight,
     pre_weight: [hidden]; gate: [hidden] (per channel) or [n_tokens, 1] (per
     token); the three share one type.  h_out may be h."""
+    if (h.requires_grad or (y is not None and y.requires_grad) or
+            (post_weight is not None and post_weight.requires_grad) or
+            (pre_weight is not None and pre_weight.requires_grad) or
+            (gate is not None and gate.requires_grad)):
+        _refuse_history("vq_block_norm", "vq_block_norm_grad")
     if h.dim() != 2:
         raise ValueError("h must be [n_tokens, hidden]")
     n, hidden = h.shape
@@ -955,6 +975,10 @@ def vq_moe_block(block: VQMoEBlock, h: torch.Tensor, attn: Optional[torch.Tensor
     """One MoE block on the fp32 residual stream h [n_tokens, hidden], in place
     (up to 64 tokens): attn (fp32) joins it first if given; returns (h, x), x
     the next block's normalised input if next_weight is given, else None."""
+    if any(t is not None and t.requires_grad
+           for t in (h, attn, attn_weight, next_weight, block.router, block.pre_weight,
+                     block.post_weight, block.channel_gate)):
+        _refuse_history("vq_moe_block")
     hidden = block.gate.cols
     if h.dim() != 2:
         raise ValueError("h must be [n_tokens, hidden]")
