@@ -288,3 +288,31 @@ def test_binding_refuses():
         vq.vq_block_norm(h[:1].expand(4, 64))
     with pytest.raises(TypeError):
         vq.vq_block_norm_grad(h, h, h.bfloat16(), h)
+
+
+@pytest.mark.parametrize("t,n", [((1 << 22) - 1, 8), (140001, 16384)])
+def test_the_most_tokens_and_offsets_past_32_bits(t, n):
+    """Every row equals the one it repeats, at the highest token counts and offsets."""
+    h, y = _r((7, n), BF, 1).cuda(), _r((7, n), BF, 2).cuda()
+    w = {k: _c(v) for k, v in _weights(n, t, BF, "channel", True, True, 0.0).items()}
+    index = torch.arange(t, device="cuda") % 7
+    big_h, big_y = h[index], y[index]
+    want = vq.vq_block_norm(h, y, **w)
+    got = vq.vq_block_norm(big_h, big_y, **w)
+    wg = vq.vq_block_norm_grad(want[0], y, want[0], want[1], **w)
+    gg = vq.vq_block_norm_grad(got[0], big_y, got[0], got[1], **w)
+    for a, b in ((got[0], want[0]), (got[1], want[1]), (gg[0], wg[0]), (gg[1], wg[1])):
+        whole = t // 7 * 7
+        assert (a[:whole].view(-1, 7, n) == b).all() and torch.equal(a[whole:], b[:t - whole])
+
+
+@pytest.mark.parametrize("hd", [F, BF])
+@pytest.mark.parametrize("yd", [F, BF])
+@pytest.mark.parametrize("xd", [F, BF])
+@pytest.mark.parametrize("wd", [F, BF])
+@pytest.mark.parametrize("t,n", [(5, 264), (3, 4104), (2, 8208)])
+def test_every_choice_of_types(hd, yd, xd, wd, t, n, monkeypatch):
+    kind = (hd, yd, xd, wd, "channel", True, True, 1.0, 0.9, 1.1)
+    monkeypatch.setitem(globals(), "KINDS", [kind])
+    test_block_norm(t, n, 0)
+    test_block_norm_grad(t, n, 0, "both")

@@ -270,3 +270,48 @@ def test_router_logits_experts_in_twos(e, hidden, n, x_dtype):
     bound = (hidden // 32 + 32 + 34) * U * (d(x).abs() @ d(w).abs().T)
     _within(got, d(x) @ d(w).T, bound, "router_logits")
     assert (buf[n * e:] == 5.0).all()
+
+
+@pytest.mark.parametrize("n,dtype", [(1, torch.bfloat16), (5, torch.float32), (64, torch.bfloat16)])
+@pytest.mark.parametrize("group", [32, 128])
+def test_the_most_columns(n, dtype, group):
+    """2^20 columns: x passes through shared memory in many chunks."""
+    rows, cols = 19, 1 << 20
+    arrays = ref.q4_make(rows, cols, group, torch.bfloat16, True, n)
+    W, x = _tensor(arrays, rows, cols, group), _x(n, cols, dtype, n)
+    y = vq.vq_q4_gemv(W, x.cuda())
+    bound = ref.q4_bound(cols, group, ref.q4_magnitude(arrays[1], arrays[2], group, x))
+    want = d(x) @ ref.q4_weights(*arrays, group).T
+    _within(y, want, bound, "most columns")
+    h = vq.vq_q4_gate_up(W, W, x.cuda())
+    s = want * torch.sigmoid(want)
+    dg = bound
+    hb = 1.1 * dg * (want.abs() + dg) + s.abs() * dg + (8 + 4 * want.abs()) * U * (s * want).abs()
+    _within(h, s * want, hb + 1e-30, "most columns, gate and up")
+
+
+@pytest.mark.parametrize("n", [1, 3, 17])
+def test_codes_past_32_bit_offsets(n):
+    """More than 2^31 words of codes (9 GB): rows on both sides of the border."""
+    rows, cols, group = 140001, 1 << 17, 128
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    codes = torch.randint(-2 ** 31, 2 ** 31 - 1, (rows, cols // 8), generator=gen, device="cuda",
+                          dtype=torch.int32)
+    scales = (0.5 + torch.rand((rows, cols // group), generator=gen, device="cuda")
+              ).to(torch.bfloat16)
+    W = vq.VQQ4Tensor(rows, cols, group, codes, scales)
+    x = _x(n, cols, torch.bfloat16, n)
+    y = vq.vq_q4_gemv(W, x.cuda()).cpu()
+    border = 2 ** 31 // (cols // 8)
+    for r in (0, border - 8, border, rows - 16):
+        part = codes[r:r + 16].cpu(), scales[r:r + 16].cpu(), None
+        bound = ref.q4_bound(cols, group, ref.q4_magnitude(part[1], None, group, x))
+        _within(y[:, r:r + 16], d(x) @ ref.q4_weights(*part, group).T, bound, f"row {r}")
+
+
+@pytest.mark.parametrize("e,hidden,n", [(1 << 20, 64, 3), (3, 1 << 20, 9), ((1 << 20) - 1, 128, 1)])
+def test_router_logits_at_its_limits(e, hidden, n):
+    w, x = _x(e, hidden, torch.bfloat16, 1), _x(n, hidden, torch.bfloat16, 2)
+    got = vq.vq_router_logits(w.cuda(), x.cuda())
+    bound = (hidden // 32 + 32 + 34) * U * (d(x).abs() @ d(w).abs().T)
+    _within(got, d(x) @ d(w).T, bound, "limits")

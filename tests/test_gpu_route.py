@@ -406,3 +406,56 @@ def test_loss_shows_a_nan():
             mask[row] = False
             loss = vq.vq_moe_route(bad.cuda(), 4, score=sigmoid, mask=mask.cuda(), balance=True)[3]
             assert torch.isfinite(loss).all()
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("t,e,k", [(37, 128, 6), (9, 512, 10), (21, 1000, 8), (5, 64, 4)])
+def test_logits_at_any_address(off, dtype, t, e, k):
+    """Logits and their gradient that start between two vectors."""
+    logits = _logits(t, e, dtype, off + e).cuda()
+    buf = torch.zeros(t * e + 16, dtype=dtype, device="cuda")
+    view = buf[off:off + t * e].view(t, e)
+    view.copy_(logits)
+    want = vq.vq_moe_route(logits, k, balance=True)
+    got = vq.vq_moe_route(view, k, balance=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    dw, dl = torch.ones_like(want[1]), torch.ones(1, device="cuda")
+    kw = dict(counts=want[2], d_loss=dl)
+    g = vq.vq_moe_route_grad(logits, want[0], dw, **kw)
+    out = torch.full((t * e + 16,), 3.0, dtype=dtype, device="cuda")
+    vq.vq_moe_route_grad(view, want[0], dw, out=out[off:off + t * e].view(t, e), **kw)
+    assert torch.equal(out[off:off + t * e].view(t, e), g)
+    assert (out[:off] == 3).all() and (out[off + t * e:] == 3).all()
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("e", [40, 70, 300])
+def test_route_special_rows_in_full(sigmoid, biased, e):
+    """Every row's ids and weights, those with scores of 0 or 1 everywhere too."""
+    k, low = 4, torch.finfo(torch.float32).min
+    rows = torch.zeros((9, e))
+    rows[0] = low
+    rows[1] = 1e30
+    rows[2] = torch.linspace(-200, -150, e)
+    rows[3, 1::2] = -0.0
+    rows[4, :] = -INF
+    rows[4, e - 1] = 1.0
+    rows[5] = low
+    rows[5, [7, e - 4]] = 3.0
+    rows[6, 5:] = -INF
+    rows[7, 3] = 1e4
+    rows[8] = torch.linspace(20, 40, e)
+    bias = torch.zeros(e) if biased else None
+    ids, w = vq.vq_moe_route(rows.cuda(), k, score=int(sigmoid), bias=_c(bias))
+    ri, rw, _, _ = ref.route(rows, k, sigmoid, bias=bias)
+    assert torch.equal(ids.cpu().long(), ri)
+    if sigmoid:
+        rw[[0, 2]] = 0.0   # below -88 a score is 0, and weights of a sum of 0 are 0
+    # exp's argument by half a step of the chosen logits' distances (0 where the
+    # result is 0), exp 2, the sum with 1, division, sum of four, division
+    sel = d(rows).gather(1, ri)
+    far = (sel[:, :1] - sel).nan_to_num(0.0, 0.0, 0.0).clamp(max=100.0)
+    err = (d(w) - rw).abs()
+    assert (err <= (far + 12) * U * rw).all(), (err / rw).max()
