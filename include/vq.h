@@ -350,7 +350,8 @@ typedef struct vq_route_config {
      counts[e] = the chosen (token, slot) pairs of expert e,
      loss = n_experts * sum_e counts[e]/(N*top_k) * (1/N) sum_t p[t][e],
    the load-balance loss over the N tokens that count (0 if N = 0), p the
-   softmax, or the sigmoid scores divided by their sum over the experts.
+   softmax, or the sigmoid scores divided by their sum over the experts, summed
+   over any number of tokens with the error of 16 fp32 additions.
    logits: device [n_tokens][n_experts] in logits_dtype; bias: device fp32
    [n_experts] or NULL, finite; mask: device uint8 [n_tokens] or NULL;
    topk_ids, topk_weights: device int32 / fp32 [n_tokens][top_k]; counts:
@@ -469,7 +470,8 @@ typedef struct vq_moe_block_args {
    [n_tokens][hidden] or NULL; attn_weight, next_weight: [hidden] in
    weight_dtype or NULL; x_next: [n_tokens][hidden] in x_dtype or NULL; all
    16-byte aligned.  n_tokens 0..64.  workspace: at least
-   vq_moe_block_workspace_size() bytes, 256-byte aligned. */
+   vq_moe_block_workspace_size() bytes, 256-byte aligned.  What a later
+   step would refuse is refused before the first one runs, with h as it was. */
 size_t vq_moe_block_workspace_size(const vq_moe_block_args *B, int32_t n_tokens);
 vq_status vq_moe_block(const vq_moe_block_args *B, int32_t n_tokens, float *h, const float *attn,
                        const void *attn_weight, const void *next_weight, void *x_next,

@@ -13,8 +13,12 @@
 //
 // One workgroup holds a token's row in registers, V groups of four values per
 // thread, so every array is read once: HBM bounds both directions (4096x4096,
-// fp32 h and y, bf16 x: 235 MB in 51 us, 4.6 TB/s; the gradient of 8191x2816 in
-// bf16: 277 MB in 64.5 us, 4.3 TB/s, and 5 us to join its partial sums).
+// fp32 h and y, bf16 x: 235 MB in 51 us, 4.6 TB/s, on outputs that are new each
+// time, 44 where the same ones stay in the 256 MB cache in part; the gradient
+// of 8191x2816 in bf16: 277 MB in 67 us, 4.2 TB/s, 5 of them to join its partial
+// sums).  Rows past 8192 do not fit the gradient's registers: 42 to 84 of a
+// thread's are in scratch (2048x16384 in bf16: 181 us, 2.2 TB/s; 2048x8192: 64,
+// 3.2 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -397,8 +401,8 @@ __global__ __launch_bounds__(64 * kFinishWaves) void k_norm_grad_finish(NormGrad
 }
 
 // Workgroups of the backward pass: two per CU (256), which is what their
-// registers leave room for (8191x2816 bf16: 64.5 us with 512, 84 with 256,
-// 81 with 1023).
+// registers leave room for (8191x2816 bf16: 71 us with 512, 93 with 256, 91 with
+// 1023; rows past 4096 have room for one: 4096x16384 310 with 512, 285 with 256).
 int grad_blocks(const vq_block_norm_args &a) { return std::min(a.n_tokens, 512); }
 
 // f(groups of four values per thread, the types of h, y and x, threads) for
@@ -433,7 +437,8 @@ hipError_t by_types(const vq_block_norm_args &a, int want, F &&f)
 hipError_t launch_block_norm(const vq_block_norm_args &a, hipStream_t stream)
 {
     // few tokens: a row over as many threads as there are, for its latency (one
-    // token of 4096: 3.9 us with 1024 threads, 4.8 with 256)
+    // token of 4096: 3.5 us with 1024 threads, 4.9 with 256; 255 tokens 5.6 and
+    // 7.7; 4096 tokens 52 and 46)
     return by_types(a, a.n_tokens < 256 ? kNormMaxThreads : 256,
                     [&](auto v, auto h, auto y, auto x, int threads) {
         k_norm<decltype(v)::value, decltype(h)::value, decltype(y)::value, decltype(x)::value>

@@ -19,11 +19,11 @@ namespace {
 //
 // logits[t][e] = sum_c w[e][c] x[t][c].  A few MB of bf16 weights: the time is
 // one trip to memory for one token (512x4096: 2.6 us, an empty launch 2.5), and
-// the reads of x from the caches for many (64 tokens of 512x4096: 9.4 us).  One
+// the reads of x from the caches for many (64 tokens of 512x4096: 10 us).  One
 // wave takes TE experts and TN tokens, its lanes eight columns at a time, so
 // that few experts still give many waves.  The sums are fp32 FMAs; matrix
 // cores, fed with 16 experts and 16 tokens straight from memory, were slower (64
-// tokens of 128x2816: 8.4 us against 5.0), for the 64 separate pieces of a load.
+// tokens of 128x2816: 8.4 us against 5), for the 64 separate pieces of a load.
 
 constexpr int kLogitWaves = 4;
 
@@ -49,8 +49,9 @@ template <int TE, int TN, bool F32>
 __global__ __launch_bounds__(64 * kLogitWaves) void k_logits(LogitsLaunch L)
 {
     // Loads of w in flight.  With fp32 or two experts one step is 10 to 18 loads
-    // already (64 fp32 tokens of 128x2816: 5.6 us with one, 6.0 with two; in bf16
-    // 5.7 and 5.0).
+    // already (64 tokens of 128x2816: fp32 6.0 us with one, 6.4 with two, bf16 6.1
+    // and 5.3; two experts of 512x4096, bf16: 10.2 and 11.0, but fp32 14.0 and
+    // 12.8).
     constexpr int kAhead = TN == 1 ? 8 : F32 || TE > 1 ? 1 : 2;
     const int lane = threadIdx.x & 63, t0 = blockIdx.y * TN;
     const int e0 =
@@ -144,9 +145,9 @@ hipError_t launch_q4(const Q4Launch &L, hipStream_t stream)
 hipError_t launch_router_logits(const LogitsLaunch &L, hipStream_t stream)
 {
     // Two experts a wave, which halves the reads of x, where that leaves waves
-    // enough for the chip (64 tokens of 512x4096: 9.4 us with two, 12.5 with one;
-    // of 128x2816: 6.2 and 5.0); for fp32, whose x is twice as long, earlier
-    // (of 256x4096: 9.8 and 11.6, in bf16 7.6 and 7.5).
+    // enough for the chip (64 tokens of 512x4096: 10.2 us with two, 13.0 with one;
+    // of 128x2816: 6.6 and 5.3); for fp32, whose x is twice as long, earlier
+    // (of 256x4096: 10.1 and 11.3, in bf16 level: 7.8 and 7.5).
     const int64_t waves = (int64_t)L.n_experts * ((L.n + 7) / 8);
     return L.n == 1 ? logits_launch<1, 1>(L, stream)
          : L.n <= 4 ? logits_launch<1, 4>(L, stream)

@@ -4,11 +4,14 @@
 //   y[t][r] = sum_g ( s[r][g] sum_{c in g} q[r][c] x[t][c] + b[r][g] sum_{c in g} x[t][c] )
 //
 // The floor is one read of the codes and scales (HBM): one token of 65541x4096
-// takes 27 us, 5.7 TB/s, 16 tokens 42, and two thousand rows the time of a
+// takes 32 us, 4.8 TB/s, 16 tokens 42, and two thousand rows the time of a
 // launch and two trips to memory (2048x2048, one token: 3.2 us).  With more
 // tokens, and three times over for fp32, reading x from LDS, unpacking and the
-// products themselves take longer than the codes (4096x4096, 64 tokens: 13 us;
-// gate and up of 8449x2816, 37 fp32 tokens: 39).  The products run on
+// products themselves take longer than the codes (4096x4096, 64 tokens: 14 us;
+// gate and up of 8449x2816, 37 fp32 tokens: 35).  (The two sides of each rule
+// below were timed in turn on one card, on weights past its 256 MB cache; from
+// card to card and with the data such times differ by up to a tenth.)  The
+// products run on
 // the matrix cores (v_mfma_f32_16x16x32_bf16: A = 16 tokens of x, B = 16 rows
 // of W), so that the vector units only turn codes into bf16, one instruction
 // per weight: a code placed in the top mantissa bits of bf16 16.0 is 16 + q
@@ -449,9 +452,10 @@ __global__ __launch_bounds__(64 * kQ4MaxWaves) void k_q4(Q4Args a)
     };
 
     // Loads return in order.  For more than four tokens x goes before the codes,
-    // so that its staging does not wait for them (4096x4096, 16 tokens: 7.1 us,
-    // else 7.9; gate and up of 2048 rows, fp32: 14.1 and 14.8); for fewer, whose
-    // x is soon there, after them (one token of 2048x2048: 3.4 us, else 4.0).
+    // so that its staging does not wait for them (16 fp32 tokens, gate and up of
+    // 2048x4096: 13.5 us, else 14.2; in bf16 this order costs 3 %: 10.0 and 9.7,
+    // 4096x4096 8.0 and 7.7); for fewer, whose x is soon there, after them (one
+    // token of 2048x2048: 3.6 us, else 3.9).
     if constexpr (kEarly) {
         fetch_x(0, first_t, first_w);
         load_block(ks);
@@ -589,11 +593,12 @@ hipError_t q4_launch(const Q4Launch &L, hipStream_t stream)
     const int tiles = (a.rows + tile_rows - 1) / tile_rows;
     const int groups = (L.n + 16 * TT - 1) / (16 * TT);   // of tokens
     // Waves per tile, which split a row: as many as keep the chip at eight waves
-    // per CU, a workgroup of eight sharing one staging of x (16 tokens, 512
-    // tiles: 15.0 us with four, 19 with eight; 4097 tiles: 43.4 with one, 45.8
-    // with two; four tokens, 4096 tiles: 32.6 with one, 49.6 with four).
-    // One token, whose x is small: eight, or four where the tiles alone fill the
-    // chip (512 tiles: 6.26 us with eight, 6.52 with four; 4097: 30.5 and 26.4).
+    // per CU, a workgroup of eight sharing one staging of x (16 tokens of 4096
+    // columns, 512 tiles: 10.4 us with four, 14.5 with eight; 4097 tiles: 45.8
+    // with one, 49.9 with two; four tokens, 4096 tiles: 32.8 with one, 38.9 with
+    // four).  One token, whose x is small: eight, or four where the tiles alone
+    // fill the chip (512 tiles: 6.8 us with eight, 7.4 with four; 1024: 11.4 and
+    // 10.2; 4097: 42.9 and 33.7).
     int ks = 3;
     if (L.n == 1)
         ks = tiles > 1024 ? 2 : 3;
@@ -616,8 +621,8 @@ hipError_t q4_launch(const Q4Launch &L, hipStream_t stream)
     // Work in whole waves per tile ends with a round that leaves CUs idle: of
     // its workgroups, where they fill half the CUs or less (or half of what
     // runs on them at once, two of half a CU's LDS), each is spread over more
-    // waves per tile (16 tokens of 4096 columns, 32784 rows: 24.6 us, else 29.4;
-    // 65541 rows: 42.4 and 47.7; gate and up of 40000 rows: 48 and 63).
+    // waves per tile (16 tokens of 4096 columns, 32784 rows: 24.4 us, else 28.9;
+    // 65541 rows: 42.2 and 46.4; gate and up of 40000 rows: 49 and 63).
     const int total = columns * groups;
     for (int slots = 256; slots <= (bytes > kQ4MaxLds / 2 ? 256 : 512); slots *= 2) {
         const int last = total % slots;
@@ -646,7 +651,7 @@ hipError_t q4_launch(const Q4Launch &L, hipStream_t stream)
     }
     // Several groups of tokens: the columns of the grid are made a multiple of
     // the eight XCDs, so that one XCD's L2 serves all groups of a tile's codes
-    // (8449x2816 gate and up, 37 fp32 tokens: 39 us, else 43).
+    // (8449x2816 gate and up, 37 fp32 tokens: 37.9 us, else 41.2).
     const dim3 grid(groups > 1 ? (columns + 7) / 8 * 8 : columns, groups);
     kern<<<grid, 64 * waves, bytes, stream>>>(a);
     return hipGetLastError();
@@ -657,18 +662,20 @@ hipError_t q4_by_tokens(const Q4Launch &L, hipStream_t stream)
 {
     // Token tiles run as workgroups of their own, which read the codes again,
     // from L2 for the most part, until they fill the chip; then a wave takes two
-    // (64 tokens of 4096 columns, 4096 rows: 11.9 us as single tiles, 12.5 in
-    // twos; 8192 rows 17.6 and 17.1; 32768 rows 60.7 and 44.8, and 46.7 in
-    // fours).  fp32, with three times the products per code, later (8192 rows:
-    // 31 us as single tiles, 35 in twos; 32768 rows: 98 and 85).
+    // (64 tokens of 4096 columns, 4096 rows: 13.6 us as single tiles, 14.3 in
+    // twos; 8192 rows 18.9 and 19.7, 16384 rows 33.8 and 32.3, 32768 rows 70 and
+    // 58).  fp32, with three times the products per code, later (8192 rows: 32
+    // us as single tiles, 36 in twos; 16384 rows 59 and 65; 32768 rows 116 and
+    // 103).
     //
     // Blocks of four units (512 columns) where there are many tiles, of two
-    // where few waves must share the latency (16 tokens, 65541 rows: 43.4 us
-    // with four, 48.4 with two; 4096 rows: 9.8 and 7.1; gate and up of 32768
-    // rows: 34.5 and 36, of 1024: 12.0 and 9.6).  For fp32, whose x takes the
-    // LDS, half of that (65541 rows: 74 us with two, 88 with four; 4096 rows:
-    // 11.8 with one, 14.8 with two).  Up to four tokens in the paired form, which
-    // has twice the codes in flight: two (8192 rows: 9.8 us, 10.8 with four).
+    // where few waves must share the latency (16 tokens, 65541 rows: 43.3 us
+    // with four, 45.5 with two; 4096 rows: 9.6 and 7.9; gate and up of 32768
+    // rows: 39 and 43, of 1024: 12.5 and 9.9).  For fp32, whose x takes the
+    // LDS, half of that (65541 rows: 79 us with two, 83 with one; 4096 rows:
+    // 13.9 and 12.2).  Up to four tokens in the paired form, which has twice the
+    // codes in flight: two (8192 rows, one token: 10.4 us, 14.2 with four; four
+    // tokens: 10.7 and 11.9).
     //
     // Two row tiles per wave in the paired form only: they halve the reads of x
     // and cost as much in occupancy.

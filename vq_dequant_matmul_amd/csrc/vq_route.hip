@@ -14,10 +14,9 @@
 // [l VPL, (l + 1) VPL), so that the lowest lane of equal keys is the lowest
 // index.  Each pass reads the logits once.  The chains of reductions and
 // exchanges within a token bound the time, not HBM: 4096 tokens of 512 experts
-// (sigmoid, bias, counts and loss, 8.7 MB) take 14 us for the selection, eight
-// waves on a CU's SIMDs, and 5 for joining the partial sums in a fixed order;
-// one token of 512 experts 4.5 us; the gradient for 16384 tokens of 128 (bf16,
-// 9.5 MB) 9.5 us, 1.0 TB/s.
+// (sigmoid, bias, counts and loss, 8.7 MB) take 19.5 us, 14 for the selection
+// and 5 for joining the partial sums in a fixed order; one token of 512 experts
+// 4.5 us; the gradient for 16384 tokens of 128 (bf16, 9.5 MB) 9.6 us, 1.0 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -31,11 +30,11 @@ namespace vq {
 namespace {
 
 constexpr int kRouteWaves = 8;      // waves per workgroup, forward (4096x512 with counts
-                                    // and loss: 8 beat 4 with half as many tokens each)
+                                    // and loss: 20.2 us, with 4 and two tokens each 22.3)
 constexpr int kGradWaves = 4;       // and backward
 constexpr int kRouteBlocks = 512;   // workgroups at most: rows of the partial sums
 constexpr int kFinishExperts = 32;  // experts of a finishing workgroup: a line of each
-                                    // row (4096x512: 14.6 us in all, 15.1 with 16, 15.9
+                                    // row (4096x512: 20.2 us in all, 20.6 with 16, 21.5
                                     // with 64)
 constexpr int kWsHeader = 2048;
 constexpr float kNegInf = -__builtin_huge_valf();
