@@ -176,3 +176,29 @@ def test_block_refuses_tensors_that_need_a_history():
     with torch.no_grad():
         got = vq.vq_moe_block(b, h, next_weight=torch.nn.Parameter(nw))
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("hidden,inter,n", [(8256, 64, 17), (16384, 64, 20), (128, 8256, 33)])
+def test_block_past_the_decode_kernels_columns(hidden, inter, n):
+    """Sizes that only the grouped GEMM takes, up to the norms' widest row."""
+    b, _, _ = _block(23, 4, 2, hidden, inter, shared_inter=64)
+    h = _r((n, hidden), F, 3).cuda()
+    want, _, _ = _by_steps(b, h.clone(), None, None, None)
+    assert torch.equal(vq.vq_moe_block(b, h)[0], want)
+
+
+def test_block_on_two_streams():
+    """Two calls at once, each with its own workspace, on the same weights."""
+    hidden, n = 512, 24
+    b, _, _ = _block(29, 16, 4, hidden, 128, shared_inter=128)
+    h = [_r((n, hidden), F, i).cuda() for i in range(2)]
+    want = [vq.vq_moe_block(b, v.clone())[0] for v in h]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    work = [[v.clone() for _ in range(6)] for v in h]
+    torch.cuda.synchronize()
+    for k in range(6):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                vq.vq_moe_block(b, work[i][k])
+    torch.cuda.synchronize()
+    assert all(torch.equal(v, want[i]) for i in range(2) for v in work[i])

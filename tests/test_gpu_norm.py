@@ -316,3 +316,22 @@ def test_every_choice_of_types(hd, yd, xd, wd, t, n, monkeypatch):
     monkeypatch.setitem(globals(), "KINDS", [kind])
     test_block_norm(t, n, 0)
     test_block_norm_grad(t, n, 0, "both")
+
+
+def test_gradients_on_two_streams():
+    """Two calls at once, each with its own workspace."""
+    t, n = 900, 2056
+    ho, y = [_r((t, n), BF, i).cuda() for i in range(2)], _r((t, n), BF, 5).cuda()
+    w = {k: _c(v) for k, v in _weights(n, t, BF, "channel", True, True, 0.0).items()}
+    want = [vq.vq_block_norm_grad(h, y, h, h, **w) for h in ho]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(6):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(vq.vq_block_norm_grad(ho[i], y, ho[i], ho[i], **w))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i]))

@@ -459,3 +459,27 @@ def test_route_special_rows_in_full(sigmoid, biased, e):
     far = (sel[:, :1] - sel).nan_to_num(0.0, 0.0, 0.0).clamp(max=100.0)
     err = (d(w) - rw).abs()
     assert (err <= (far + 12) * U * rw).all(), (err / rw).max()
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_loss_of_a_long_batch_repeats(sigmoid):
+    """More tokens than a wave's first sixteen: the same bits eagerly, again, and in
+    a graph whose inputs change, and the loss of the definition."""
+    t, e, k = 70001, 130, 5
+    logits = _logits(t, e, torch.float32, 9).cuda()
+    mask = _mask(t, 3).cuda()
+    kw = dict(score=int(sigmoid), mask=mask, balance=True)
+    first = vq.vq_moe_route(logits, k, **kw)
+    _, _, counts, loss = ref.route(logits.cpu(), k, sigmoid, mask=mask.cpu())
+    assert torch.equal(first[2].cpu().long(), counts)
+    # p: its exponentials (4, and half a step of a distance of 20 at most), its sum and
+    # product, a sum of 16; two roundings of the sums
+    assert abs(float(first[3]) - float(loss)) <= (20 + 8 + e / 64 + 6 + 4 + 16 + 2) * U * float(loss)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = vq.vq_moe_route(logits, k, **kw)
+    for i in range(3):
+        logits.copy_(_logits(t, e, torch.float32, 30 + i))
+        g.replay()
+        for a, b in zip(out, vq.vq_moe_route(logits, k, **kw)):
+            assert torch.equal(a, b), i
