@@ -285,8 +285,8 @@ vq_status vq_moe_stack(const vq_moe_layer *layers, int32_t n_layers, int32_t n_t
    q = the 4-bit code: bits [4*(c%8), 4*(c%8)+4) of word c/8 of row r. */
 typedef struct vq_q4_tensor {
     int32_t rows;          /* out features, 1..2^27                           */
-    int32_t cols;          /* in features, a positive multiple of group and
-                              64, at most 2^20                                */
+    int32_t cols;          /* in features, a positive multiple of group, at
+                              most 2^20                                       */
     int32_t group;         /* weights per scale along a row: 32, 64 or 128    */
     vq_dtype scale_dtype;  /* VQ_F16 or VQ_BF16: type of scales and biases    */
     const uint32_t *codes; /* device [rows][cols/8], 16-byte aligned          */

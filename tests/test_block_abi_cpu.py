@@ -367,3 +367,40 @@ def test_binding_without_grad_takes_parameters():
         for call in (lambda: vq.vq_block_norm(h), lambda: vq.vq_moe_route(h, 2)):
             with pytest.raises((TypeError, RuntimeError)):
                 call()
+
+
+@pytest.mark.parametrize("cols", [32, 96, 160, 4128])
+def test_q4_any_whole_number_of_groups(lib, cols):
+    t = _q4(cols=cols, group=32)
+    assert lib.vq_q4_gemv(ctypes.byref(t), 0, None, 1, None, 0, None) == 0
+    assert lib.vq_q4_gate_up(ctypes.byref(t), ctypes.byref(t), 0, None, 1, None, None) == 0
+    vq.VQQ4Tensor(4, cols, 32, torch.zeros((4, cols // 8), dtype=torch.int32),
+                  torch.zeros((4, cols // 32), dtype=torch.float16))
+    _refused(lib, lib.vq_q4_gemv(ctypes.byref(_q4(cols=cols, group=64)), 1, FAKE, 1, FAKE, 0, None),
+             1, "cols")
+
+
+def test_the_measured_ranges_are_accepted(lib):
+    """Every case that perf/operators.py can give passes the host's checks of sizes."""
+    import random
+
+    import perf.operators as ops
+    for c in ops.listed() + [ops.draw(random.Random(i)) for i in range(1000)]:
+        op = c["op"]
+        if op in ("q4_gemv", "q4_gate_up"):
+            t = ctypes.byref(_q4(rows=c["rows"], cols=c["cols"], group=c["group"],
+                                 biases=FAKE if c["affine"] else None))
+            assert lib.vq_q4_gemv(t, 0, None, 1, None, 0, None) == 0, c
+            assert 1 <= c["tokens"] <= 64
+        elif op == "logits":
+            assert lib.vq_router_logits(c["experts"], c["hidden"], FAKE, 0, None, 1, None,
+                                        None) == 0, c
+            assert 1 <= c["tokens"] <= 64
+        elif op in ("route", "route_grad"):
+            r = ctypes.byref(_route(n_experts=c["experts"], top_k=c["k"]))
+            assert lib.vq_moe_route_workspace_size(r, c["tokens"]) > 0, c
+        else:
+            n = c["hidden"]
+            a = _norm(n_tokens=c["tokens"], hidden=n, h_stride=n, y_stride=n, h_out_stride=n,
+                      x_stride=n)
+            assert lib.vq_block_norm_grad_workspace_size(ctypes.byref(a)) > 0, c

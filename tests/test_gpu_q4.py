@@ -315,3 +315,29 @@ def test_router_logits_at_its_limits(e, hidden, n):
     got = vq.vq_router_logits(w.cuda(), x.cuda())
     bound = (hidden // 32 + 32 + 34) * U * (d(x).abs() @ d(w).abs().T)
     _within(got, d(x) @ d(w).T, bound, "limits")
+
+
+@pytest.mark.parametrize("cols", [32, 96, 160, 608, 2080, 4128])
+@pytest.mark.parametrize("rows,n", [(1, 1), (37, 4), (300, 2), (45, 17), (520, 64), (16500, 16),
+                                    (33000, 20)])
+@pytest.mark.parametrize("x_dtype,scale_dtype,affine", [
+    (torch.bfloat16, torch.float16, True), (torch.float32, torch.bfloat16, False)])
+def test_any_whole_number_of_groups(cols, rows, n, x_dtype, scale_dtype, affine):
+    """Groups of 32 whose number is odd: rows of codes that end inside a unit of 128
+    columns and of a load, scales that start between words; nothing behind is touched."""
+    group = 32
+    ga, ua = (ref.q4_make(rows, cols, group, scale_dtype, affine, rows + cols + i)
+              for i in (0, 1))
+    G, UP = _tensor(ga, rows, cols, group), _tensor(ua, rows, cols, group)
+    x = _x(n, cols, x_dtype, n)
+    buf = torch.full(((n + 1) * rows,), 3.0, device="cuda")
+    out, behind = buf[:n * rows].view(n, rows), buf[n * rows:]
+    vq.vq_q4_gemv(G, x.cuda(), out=out)
+    g, u = (d(x) @ ref.q4_weights(*a, group).T for a in (ga, ua))
+    dg, du = (ref.q4_bound(cols, group, ref.q4_magnitude(a[1], a[2], group, x)) for a in (ga, ua))
+    _within(out, g, dg, "gemv")
+    vq.vq_q4_gate_up(G, UP, x.cuda(), out=out)
+    s = g * torch.sigmoid(g)
+    bound = 1.1 * dg * (u.abs() + du) + s.abs() * du + (8 + 4 * g.abs()) * U * (s * u).abs()
+    _within(out, s * u, bound + 1e-30, "gate and up")
+    assert (behind == 3.0).all()

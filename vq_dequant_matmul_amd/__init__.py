@@ -609,8 +609,8 @@ class VQQ4Tensor:
     biases: Optional[torch.Tensor] = None
 
     def __post_init__(self):
-        if self.group not in (32, 64, 128) or self.cols % max(self.group, 64) != 0:
-            raise ValueError("group must be 32, 64 or 128 and cols a multiple of it and of 64")
+        if self.group not in (32, 64, 128) or self.cols % self.group != 0:
+            raise ValueError("group must be 32, 64 or 128 and cols a multiple of it")
         if self.codes.dtype != torch.int32 or tuple(self.codes.shape) != (self.rows,
                                                                            self.cols // 8):
             raise ValueError(f"codes must be int32 [{self.rows}, {self.cols // 8}]")

@@ -35,10 +35,10 @@ vq_status check_q4(const vq_q4_tensor *t, const char *name)
     if (t->group != 32 && t->group != 64 && t->group != 128)
         return fail(VQ_ERR_UNSUPPORTED, "%s.group = %d: supported group sizes are 32, 64 and 128",
                     name, t->group);
-    if (t->cols < 64 || t->cols % 64 != 0 || t->cols % t->group != 0)
+    if (t->cols < t->group || t->cols % t->group != 0)
         return fail(VQ_ERR_INVALID_ARGUMENT,
-                    "%s.cols = %d: must be a positive multiple of 64 and of group = %d", name,
-                    t->cols, t->group);
+                    "%s.cols = %d: must be a positive multiple of group = %d", name, t->cols,
+                    t->group);
     if (t->scale_dtype != VQ_F16 && t->scale_dtype != VQ_BF16)
         return fail(VQ_ERR_INVALID_ARGUMENT, "%s.scale_dtype = %d: must be VQ_F16 or VQ_BF16",
                     name, (int)t->scale_dtype);
