@@ -483,3 +483,21 @@ def test_loss_of_a_long_batch_repeats(sigmoid):
         g.replay()
         for a, b in zip(out, vq.vq_moe_route(logits, k, **kw)):
             assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("e", [10, 72, 200, 519, 764])
+def test_gradient_of_a_single_renormalised_choice(sigmoid, dtype, e):
+    """One slot's renormalised weight is 1 whatever the logits: its gradient is 0, and
+    with the loss the gradient is that of the loss alone."""
+    t = 203
+    logits = _logits(t, e, dtype, e).cuda()
+    ids, w, counts, _ = vq.vq_moe_route(logits, 1, score=int(sigmoid), balance=True)
+    assert (w == 1).all()
+    dw = _logits(t, 1, torch.float32, 2).cuda()
+    kw = dict(score=int(sigmoid), scale=2.5)
+    assert (vq.vq_moe_route_grad(logits, ids, dw, **kw) == 0).all()
+    loss = dict(counts=counts, d_loss=torch.tensor([0.3]).cuda())
+    assert torch.equal(vq.vq_moe_route_grad(logits, ids, dw, **kw, **loss),
+                       vq.vq_moe_route_grad(logits, ids, None, **kw, **loss))

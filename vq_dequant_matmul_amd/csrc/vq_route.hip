@@ -791,7 +791,10 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_route_grad(RouteGradLaunch 
             const float over = tot == 0.0f ? 0.0f : 1.0f / tot;
 #pragma unroll
             for (int i = 0; i < KPL; ++i) {
-                w[i] *= over;
+                // the quotient with its remainder: the one weight of a single slot is
+                // 1, and its gradient 0
+                const float v = w[i] * over;
+                w[i] = fmaf(fmaf(-v, tot, w[i]), over, v);
                 mean += g[i] * w[i];
             }
             mean = segment_sum<S>(mean);
