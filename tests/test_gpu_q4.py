@@ -341,3 +341,21 @@ def test_any_whole_number_of_groups(cols, rows, n, x_dtype, scale_dtype, affine)
     bound = 1.1 * dg * (u.abs() + du) + s.abs() * du + (8 + 4 * g.abs()) * U * (s * u).abs()
     _within(out, s * u, bound + 1e-30, "gate and up")
     assert (behind == 3.0).all()
+
+
+@pytest.mark.parametrize("group,cols", [(32, 512), (64, 512), (64, 1088), (128, 512), (128, 640),
+                                        (128, 1536)])
+@pytest.mark.parametrize("rows,n", [(4000, 1), (4000, 3), (700, 11), (3000, 34), (17000, 64)])
+def test_fp32_activations_keep_their_digits(group, cols, rows, n):
+    """The error as a norm over all outputs, where roundings add as independent ones.
+
+    Codes enter as 16 + q, 24 times the scale in the mean, and weights are 4.6 scales in
+    the root mean square, so a rounding of a group's sum weighs 5.2 times.  Six roundings
+    (a step per 32 columns of the highest term, two where it meets the rest) of the
+    products' sum and of x's, U / sqrt(3) each: 2 * 5.2 U; the sum over the groups adds
+    less than 1.5 U."""
+    arrays = ref.q4_make(rows, cols, group, torch.bfloat16, False, cols + n)
+    x = _x(n, cols, torch.float32, n)
+    y = d(vq.vq_q4_gemv(_tensor(arrays, rows, cols, group), x.cuda()))
+    want = d(x) @ ref.q4_weights(*arrays, group).T
+    assert (y - want).norm() <= 12 * U * want.norm()

@@ -201,8 +201,10 @@ struct Q4Lds {
 // quarter t%4, so up to four tokens need one).  TL row tiles per wave: rows r
 // and r + 16, or the same rows of gate and up.  SU units per block, the piece
 // of 16 rows that a wave has in flight.  SB: bf16 scales, AF: biases.
+// (Groups of 128 with two token tiles: 128 registers, so that a CU holds two
+// workgroups; 64 fp32 tokens of 32768x4096: 103 us, else 113.)
 template <int G, int PL, int TT, int NI, int TL, int SU, bool SB, bool AF>
-__global__ __launch_bounds__(64 * kQ4MaxWaves) void k_q4(Q4Args a)
+__global__ __launch_bounds__(64 * kQ4MaxWaves, G == 128 && TT == 2 && TL == 1 ? 4 : 2) void k_q4(Q4Args a)
 {
     using S = Q4Lds<G, SU, TL>;
     constexpr int NG = 128 / G;        // groups of a unit
@@ -408,27 +410,62 @@ __global__ __launch_bounds__(64 * kQ4MaxWaves) void k_q4(Q4Args a)
             }
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
+                // The lower terms of x are summed first: next to the sums of the highest
+                // one each of their steps would round as much as it adds (error of 640
+                // columns in groups of 128: 2.4e-7, else 1.4e-6).  That keeps a group's
+                // unpacked codes in registers; with few tokens, whose x is read ahead
+                // into them, lower sums apart cost less (one token of 65536x4096: groups
+                // of 64 49 us, else 63, of 128 50 and 60; of 32, one operand a group, 50
+                // and 51).
                 f32x4 acc[TL][TT] = {}, xs[TT] = {};
-#pragma unroll
-                for (int m = 0; m < 4 / NG; ++m) {
+                const auto step_of = [&](int pl, int m, const bf16x8 (&wv)[TL],
+                                         f32x4 (&to)[TL][TT], f32x4 (&xt)[TT]) {
                     const int slot = g * (4 / NG) + m;
-                    bf16x8 wv[TL];
+#pragma unroll
+                    for (int tt = 0; tt < TT; ++tt) {
+                        const bf16x8 av = __builtin_bit_cast(
+                            bf16x8, xa[((pl * cu + uc) * 16 + slot * 4 + q) * np + tok[tt]]);
+                        xt[tt] =
+                            __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, ones, xt[tt], 0, 0, 0);
+#pragma unroll
+                        for (int l = 0; l < TL; ++l)
+                            to[l][tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                av, wv[l], to[l][tt], 0, 0, 0);
+                    }
+                };
+                bf16x8 wv[4 / NG][TL];
+                const auto unpack_slot = [&](int m) {
 #pragma unroll
                     for (int l = 0; l < TL; ++l)
-                        wv[l] = unpack(ww[l][slot], mask, base);
+                        wv[m][l] = unpack(ww[l][g * (4 / NG) + m], mask, base);
+                };
+                if constexpr (PL > 1 && NI == 1 && G > 32) {
+                    f32x4 low[TL][TT] = {}, xl[TT] = {};
 #pragma unroll
-                    for (int pl = 0; pl < PL; ++pl)
+                    for (int m = 0; m < 4 / NG; ++m) {
+                        unpack_slot(m);
+                        step_of(0, m, wv[m], acc, xs);
 #pragma unroll
-                        for (int tt = 0; tt < TT; ++tt) {
-                            const bf16x8 av = __builtin_bit_cast(
-                                bf16x8,
-                                xa[((pl * cu + uc) * 16 + slot * 4 + q) * np + tok[tt]]);
-                            xs[tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, ones, xs[tt],
-                                                                             0, 0, 0);
+                        for (int pl = 1; pl < PL; ++pl)
+                            step_of(pl, m, wv[m], low, xl);
+                    }
+#pragma unroll
+                    for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                        for (int i = 0; i < NI; ++i) {
+                            xs[tt][i] += xl[tt][i];
 #pragma unroll
                             for (int l = 0; l < TL; ++l)
-                                acc[l][tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                    av, wv[l], acc[l][tt], 0, 0, 0);
+                                acc[l][tt][i] += low[l][tt][i];
+                        }
+                } else {
+#pragma unroll
+                    for (int pl = PL - 1; pl >= 0; --pl)
+#pragma unroll
+                        for (int m = 0; m < 4 / NG; ++m) {
+                            if (pl == PL - 1)
+                                unpack_slot(m);
+                            step_of(pl, m, wv[m], acc, xs);
                         }
                 }
                 float sv[TL], cv[TL];
