@@ -8,7 +8,7 @@
 // launch and two trips to memory (2048x2048, one token: 3.2 us).  With more
 // tokens, and three times over for fp32, reading x from LDS, unpacking and the
 // products themselves take longer than the codes (4096x4096, 64 tokens: 14 us;
-// gate and up of 8449x2816, 37 fp32 tokens: 35).  (The two sides of each rule
+// gate and up of 8449x2816, 37 fp32 tokens: 36).  (The two sides of each rule
 // below were timed in turn on one card, on weights past its 256 MB cache; from
 // card to card and with the data such times differ by up to a tenth.)  The
 // products run on
