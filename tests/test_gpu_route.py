@@ -501,3 +501,30 @@ def test_gradient_of_a_single_renormalised_choice(sigmoid, dtype, e):
     loss = dict(counts=counts, d_loss=torch.tensor([0.3]).cuda())
     assert torch.equal(vq.vq_moe_route_grad(logits, ids, dw, **kw, **loss),
                        vq.vq_moe_route_grad(logits, ids, None, **kw, **loss))
+
+
+@pytest.mark.parametrize("e", [5, 400, 1000])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_loss_of_a_long_batch_at_every_width(e, dtype, sigmoid):
+    """Past a wave's first sixteen tokens, p summed in 64 bits on the device; a NaN of
+    an early token that counts shows, of one that does not, not."""
+    t, k = 131073, 3
+    logits = _logits(t, e, dtype, e).cuda()
+    mask = _mask(t, 4).cuda()
+    mask[17] = True
+    kw = dict(score=int(sigmoid), balance=True)
+    _, _, counts, loss = vq.vq_moe_route(logits, k, mask=mask, **kw)
+    total = torch.zeros(e, dtype=torch.float64, device="cuda")
+    for part, live in zip(logits.split(8192), mask.split(8192)):
+        total += ref.scores(part[live].double(), sigmoid)[1].sum(0)
+    n = int(mask.sum())
+    assert int(counts.sum()) == n * k
+    want = e * float((counts.double() * total).sum()) / (n * k) / n
+    # p: as exact as a weight, whose bound is the largest here; 16 additions, two roundings
+    # of sums
+    assert abs(float(loss) - want) <= (20 + 8 + e / 64 + 6 + 4 + 16 + 2) * U * want
+    logits[17, 2] = NAN
+    assert vq.vq_moe_route(logits, k, mask=mask, **kw)[3].isnan().all()
+    mask[17] = False
+    assert torch.isfinite(vq.vq_moe_route(logits, k, mask=mask, **kw)[3]).all()
